@@ -219,21 +219,13 @@ __device__ inline void each_entry(const Teacher& s, int k, uint32_t lo, uint32_t
   else pass(std::integral_constant<int, 4>{});
 }
 
-// exp2(x * c + b) = exp((x - shift) / tau).  The rounding of b is common to a row's
-// exponentials and their sum.  Where it would overflow, every logit is huge, and two
-// that differ at all differ by far more than an exponent can hold: any smaller factor
-// then gives the same 0 or 1.
+// exp((x - shift) / tau).  The difference is taken first, so it is exact near the maximum
+// whatever the logits' common offset.  (As x * c - shift * c in one instruction, what the two
+// products' roundings leave grows with the offset: in a row of -1e9 a factor of 2^18.)
 struct Exponent {
-  float c, b;
-  __device__ Exponent(float shift, float inv_tau, float scaled_shift) {
-    c = LOG2E * inv_tau;
-    b = -scaled_shift * LOG2E;
-    if (__builtin_isinf(b) && !__builtin_isinf(shift)) {
-      c = inv_tau * 0x1p-64f;
-      b = -scaled_shift * 0x1p-64f;
-    }
-  }
-  __device__ inline float operator()(float x) const { return fast_exp2(__builtin_fmaf(x, c, b)); }
+  float shift, c;
+  __device__ Exponent(float at, float inv_tau) : shift(at), c(LOG2E * inv_tau) {}
+  __device__ inline float operator()(float x) const { return fast_exp2((x - shift) * c); }
 };
 
 enum DistillMode { D_FWD = 0, D_BOTH = 1 };
@@ -320,7 +312,7 @@ void k_distill(DistillArgs a) {
   const float own_max = m2[0];
   block_all<NT>(m2, 2, scratch, OpMax());
   const float xm = m2[0] == NINF ? 0.f : m2[0], tmax = m2[1] == NINF ? 0.f : m2[1];
-  const Exponent ex(xm, inv_tau, xm * inv_tau);
+  const Exponent ex(xm, inv_tau);
   // the pieces as they were loaded: without this the compiler keeps the unpacked values
   // of one pass for the next, which do not fit the registers
   auto repack = [&]() {
@@ -447,8 +439,8 @@ __global__ __launch_bounds__(NT) void k_distill_backward(DistillArgs a) {
   block_all<NT>(S, 1, scratch, OpSum());
   const bool live = S[0] != 0.f;
   const float g = live ? a.tau * a.row_grad[r] : 0.f, gp = live ? g / S[0] : 0.f;
-  const Exponent ex(lse, inv_tau, lse);
-  auto q_of = [&](float x) { return live ? ex(x) * g : 0.f; };
+  // exp(x / tau - lse)
+  auto q_of = [&](float x) { return live ? fast_exp2(__builtin_fmaf(x, inv_tau, -lse) * LOG2E) * g : 0.f; };
   if (row.F > 0)
 #pragma unroll
     for (int q = 0; q < NV; ++q) {
