@@ -293,7 +293,7 @@ int32_t mo_expert_weight_grad(const void *dy, int64_t lddy, const void *x, int64
  * A row without entries, or whose entries are all -inf, has loss 0 and a zero grad.
  * Entries of one row that name the same id count one by one in the loss and add up in
  * the gradient.  grad is written whole, in the logits' dtype, rows ldg values apart;
- * it must not overlap the logits.  1 <= k <= 1024, temperature > 0, vocab <= 2^28.
+ * it must not overlap the logits (MO_ERR_INVALID).  1 <= k <= 1024, temperature > 0, vocab <= 2^28.
  * mo_distill_backward takes the lse of mo_distill_forward;
  * mo_distill_forward_backward does both in one pass over the logits. */
 int32_t mo_distill_forward(const void *logits, int64_t ldx, const void *indices, int32_t index_bytes,

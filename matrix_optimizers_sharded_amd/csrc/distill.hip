@@ -26,6 +26,15 @@ int check_distill(const void* logits, int64_t ldx, const void* ids, int32_t id_b
   return MO_OK;
 }
 
+int check_grad(const void* logits, int64_t ldx, const void* grad, int64_t ldg, int64_t n, int64_t vocab,
+               int32_t dtype) {
+  const int64_t es = static_cast<int64_t>(dtype_size(dtype));
+  const __int128 px = ldx, pg = ldg;
+  if (overlap({logits, n, vocab * es, px * es}, {grad, n, vocab * es, pg * es}))
+    return fail(MO_ERR_INVALID, "grad must not be logits, nor overlap them");
+  return MO_OK;
+}
+
 template <typename T, int MODE>
 int run_rows(const DistillArgs& a, hipStream_t stream) {
   const int64_t pieces = a.V / RowVec<T>::N;
@@ -101,6 +110,7 @@ int32_t mo_distill_backward(const void* logits, int64_t ldx, const float* lse, c
     if (ldg < vocab) return fail(MO_ERR_INVALID, "grad: the row pitch must be >= vocab");
     if (n == 0) return MO_OK;
     if (!lse || !row_grad || !grad) return fail(MO_ERR_INVALID, "lse, row_grad or grad is NULL");
+    MO_TRY(check_grad(logits, ldx, grad, ldg, n, vocab, dtype));
     DistillArgs a = {logits, ldx, indices, teacher, vocab, n, static_cast<int>(k), index_bytes == 8, temperature,
                      row_grad, lse, nullptr, nullptr, grad, ldg};
     if (dtype == MO_F32) return run_backward<float>(a, static_cast<hipStream_t>(stream));
@@ -117,7 +127,7 @@ int32_t mo_distill_forward_backward(const void* logits, int64_t ldx, const void*
     if (ldg < vocab) return fail(MO_ERR_INVALID, "grad: the row pitch must be >= vocab");
     if (n == 0) return MO_OK;
     if (!loss || !lse || !row_grad || !grad) return fail(MO_ERR_INVALID, "loss, lse, row_grad or grad is NULL");
-    if (grad == logits) return fail(MO_ERR_INVALID, "grad must not be logits");
+    MO_TRY(check_grad(logits, ldx, grad, ldg, n, vocab, dtype));
     DistillArgs a = {logits, ldx, indices, teacher, vocab, n, static_cast<int>(k), index_bytes == 8, temperature,
                      row_grad, nullptr, loss, lse, grad, ldg};
     if (dtype == MO_F32) return run_rows<float, D_BOTH>(a, static_cast<hipStream_t>(stream));

@@ -30,6 +30,23 @@ inline size_t dtype_size(int dt) { return dt == MO_F32 ? 4 : 2; }
 inline bool valid_dtype(int dt) { return dt == MO_F32 || dt == MO_BF16; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// `rows` rows of `width` bytes, `pitch` bytes apart.
+struct ByteRows {
+  const void* p;
+  int64_t rows, width;
+  __int128 pitch;   // any pitch in elements fits
+};
+// Whether two of them share memory.  Columns of one buffer side by side do not.
+inline bool overlap(const ByteRows& a, const ByteRows& b) {
+  if (a.rows <= 0 || b.rows <= 0) return false;
+  auto first = [](const ByteRows& r) { return static_cast<__int128>(reinterpret_cast<uintptr_t>(r.p)); };
+  auto end = [&](const ByteRows& r) { return first(r) + (r.rows - 1) * r.pitch + r.width; };
+  if (end(a) <= first(b) || end(b) <= first(a)) return false;
+  if (a.pitch != b.pitch) return true;
+  const __int128 apart = ((first(b) - first(a)) % a.pitch + a.pitch) % a.pitch;
+  return apart < a.width || apart + b.width > a.pitch;
+}
+
 // ---- optional per-kernel timing ------------------------------------------------
 struct ProfRec {
   int kind;

@@ -287,7 +287,8 @@ def distill_forward(logits, indices, teacher, temperature=1.0):
 
 
 def distill_backward(logits, lse, indices, teacher, row_grad, temperature=1.0, out=None):
-    """Gradient of the logits for the rows' weights row_grad, from distill_forward's lse."""
+    """Gradient of the logits for the rows' weights row_grad, from distill_forward's lse.
+    Not in place: out must not overlap the logits."""
     dev, ld, ib, n, v, k, code = _distill(logits, indices, teacher, temperature, lse, row_grad)
     out = _result(out, (n, v), logits.dtype, dev, "out")
     _run("mo_distill_backward", dev, logits.data_ptr(), ld, lse.data_ptr(), indices.data_ptr(), ib,
@@ -296,7 +297,8 @@ def distill_backward(logits, lse, indices, teacher, row_grad, temperature=1.0, o
 
 
 def distill_forward_backward(logits, indices, teacher, row_grad, temperature=1.0, out=None):
-    """(loss, lse, gradient of the logits) in one pass, where the rows' weights are known."""
+    """(loss, lse, gradient of the logits) in one pass, where the rows' weights are known.
+    Not in place: out must not overlap the logits."""
     dev, ld, ib, n, v, k, code = _distill(logits, indices, teacher, temperature, None, row_grad)
     loss, lse = teacher.new_empty(n), teacher.new_empty(n)
     out = _result(out, (n, v), logits.dtype, dev, "out")

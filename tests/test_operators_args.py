@@ -177,3 +177,27 @@ def test_expert_products_refuse_rows_past_32_bits():
         for n in ((1 << 31) - 1023, (1 << 31) - 1, 1 << 31, -1):
             b = [n if v is None and i in (5, 6) else v for i, v in enumerate(a)]
             refused(INVALID, "n must be", name, *b)
+
+
+def test_distill_refuses_a_gradient_over_the_logits():
+    """The kernels read a row's logits again after they have stored its gradient."""
+    n, v = 4, 100
+    shape = [n, v, 8, 0, ctypes.c_float(1.0)]
+
+    def args(name, logits, ld, grad, ldg):
+        if name == "mo_distill_backward":
+            return [logits, ld, 0x1000, 0x2000, 8, 0x3000, 0x4000] + shape + [grad, ldg, None]
+        return [logits, ld, 0x2000, 8, 0x3000, 0x4000] + shape + [0x5000, 0x6000, grad, ldg, None]
+
+    at = 0x100000
+    for f in ("mo_distill_backward", "mo_distill_forward_backward"):
+        for logits, ld, grad, ldg in ((at, 100, at, 100), (at, 100, at + 400, 100), (at + 1596, 100, at, 100),
+                                      (at, 100, at + 1596, 250), (at, 250, at + 396, 250), (at + 396, 250, at, 250),
+                                      (at, 1 << 61, at + 4, 100)):
+            refused(INVALID, "grad must not be logits", f, *args(f, logits, ld, grad, ldg))
+        # side by side, and one behind the other: past this check (and then, without a GPU or
+        # with no rows, no further)
+        for logits, ld, grad, ldg in ((at, 250, at + 400, 250), (at + 600, 250, at, 250), (at, 100, at + 1600, 100)):
+            a = args(f, logits, ld, grad, ldg)
+            if not torch.cuda.is_available():
+                assert call(f, *a) != INVALID, error()
