@@ -294,7 +294,10 @@ int32_t mo_expert_weight_grad(const void *dy, int64_t lddy, const void *x, int64
  * Entries of one row that name the same id count one by one in the loss and add up in
  * the gradient.  grad is written whole, in the logits' dtype, rows ldg values apart;
  * it must not overlap the logits (MO_ERR_INVALID).  1 <= k <= 1024, temperature > 0, vocab <= 2^28.
- * mo_distill_backward takes the lse of mo_distill_forward;
+ * lse is rounded to fp32 (an infinity where it lies beyond).  A common offset of a row's
+ * logits, exact in their dtype, changes neither loss nor gradient.
+ * mo_distill_backward takes the lse of mo_distill_forward; a row whose lse is 1024 or more
+ * in size is summed again, since fp32 holds it too coarsely there.
  * mo_distill_forward_backward does both in one pass over the logits. */
 int32_t mo_distill_forward(const void *logits, int64_t ldx, const void *indices, int32_t index_bytes,
                            const float *teacher, int64_t n, int64_t vocab, int64_t k, int32_t dtype,

@@ -408,6 +408,41 @@ void k_distill(DistillArgs a) {
   }
 }
 
+// A row's maximum (0 for a row of -inf) and sum of exponentials, by a block that holds
+// nothing of it.
+template <typename T, int NT>
+__device__ inline void row_sum(const Row<T>& row, float inv_tau, float (*scratch)[16], float& m, float& sum) {
+  constexpr int N = RowVec<T>::N;
+  const uint32_t tid = threadIdx.x;
+  const float xr = row.load_rest(tid);
+  float v[1] = {xr};
+  for (uint32_t i = tid; i < row.F; i += NT) {
+    float f[N];
+    unpack<T>(row.load(i), f);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[0] = fmaxf(v[0], f[k]);
+  }
+  block_all<NT>(v, 1, scratch, OpMax());
+  m = v[0] == -__builtin_inff() ? 0.f : v[0];
+  const Exponent ex(m, inv_tau);
+  v[0] = ex(xr);
+  for (uint32_t i = tid; i < row.F; i += NT) {
+    float f[N];
+    unpack<T>(row.load(i), f);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[0] += ex(f[k]);
+  }
+  block_all<NT>(v, 1, scratch, OpSum());
+  sum = v[0];
+}
+
+// From this size on the pass from lse sums a row anew: half of fp32's step, the error of the
+// exponent, is 2^-15 below, and at 1e7 a factor of 1.6.  Logits that large come from masks
+// (-1e9, the type's lowest value) in rows that are masked whole, and from temperatures of
+// 0.01.  Every part of such a row reads all of it: rows of 32768 bf16 logits take twice the
+// time, rows of 131072 six times.
+constexpr float LSE_FINE = 1024.f;
+
 // The backward pass from the forward's lse: block (part, row) stores NT * NV pieces.
 template <typename T, int NT, int NV>
 __global__ __launch_bounds__(NT) void k_distill_backward(DistillArgs a) {
@@ -439,8 +474,18 @@ __global__ __launch_bounds__(NT) void k_distill_backward(DistillArgs a) {
   block_all<NT>(S, 1, scratch, OpSum());
   const bool live = S[0] != 0.f;
   const float g = live ? a.tau * a.row_grad[r] : 0.f, gp = live ? g / S[0] : 0.f;
-  // exp(x / tau - lse)
-  auto q_of = [&](float x) { return live ? fast_exp2(__builtin_fmaf(x, inv_tau, -lse) * LOG2E) * g : 0.f; };
+  // exp((x * by - at) * c) * gq: exp(x / tau - lse) * g; or, where fp32 holds lse too
+  // coarsely, exp((x - max) / tau) * g / sum, from the row itself.
+  float by = inv_tau, at = lse, c = LOG2E, gq = g;
+  if (live && !(fabsf(lse) < LSE_FINE)) {
+    float m, sum;
+    row_sum<T, NT>(row, inv_tau, scratch, m, sum);
+    by = 1.f;
+    at = m;
+    c = LOG2E * inv_tau;
+    gq = g / sum;
+  }
+  auto q_of = [&](float x) { return live ? fast_exp2(__builtin_fmaf(x, by, -at) * c) * gq : 0.f; };
   if (row.F > 0)
 #pragma unroll
     for (int q = 0; q < NV; ++q) {

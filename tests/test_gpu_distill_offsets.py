@@ -105,3 +105,38 @@ def test_rows_of_one_value(gpu, dtype, v, value, tau):
         assert bool((lse == math.copysign(math.inf, want)).all())
     else:
         close(lse, torch.full((4,), want, dtype=F64, device=gpu), torch.tensor(abs(want) * 4 * U32, device=gpu), "lse")
+
+
+@pytest.mark.parametrize("tau", [0.5, 1.0, 1.7, 2.0])
+@pytest.mark.parametrize("value", VALUES)
+@pytest.mark.parametrize("v", LENGTHS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradient_from_lse_of_rows_of_one_value(gpu, dtype, v, value, tau):
+    value = value_of(value, dtype)
+    x, idx, t, rg, tau32, _, want, tol = constant_rows(gpu, v, dtype, value, tau)
+    _, lse = mo.distill_forward(x, idx, t, temperature=tau)
+    grad = mo.distill_backward(x, lse, idx, t, rg, temperature=tau)
+    close(grad, want, tol[1], "gradient from lse")
+    assert not grad[0].any()
+
+
+@pytest.mark.parametrize("v", LENGTHS)
+@pytest.mark.parametrize("dtype,unit,offset,tau", OFFSETS + [(F32, 0.125, 900.0, 1.0), (F32, 0.125, -1100.0, 1.0)])
+def test_gradient_from_lse_with_an_offset(gpu, dtype, unit, offset, tau, v):
+    """Where lse is below 1024 in size, its own rounding and that of x / tau are an error of the
+    exponent; beyond, the result is as exact as without an offset."""
+    say(f"distill_backward offset {offset} v={v} {dtype}")
+    plain, moved = shifted(gpu, v, dtype, unit, offset, v)
+    idx, t, rg = teacher_rows(gpu, 4, v, 9, v + 1)
+    tau32 = float(torch.tensor(tau, dtype=F32))
+    _, _, want, q, whole = distill_exact(plain, idx, t, rg, tau32)
+    _, lse = mo.distill_forward(moved, idx, t, temperature=tau)
+    grad = mo.distill_backward(moved, lse, idx, t, rg, temperature=tau)
+    reach = 63 * unit / tau * 1.4427
+    rt = (3 * float(t.amax() - t.amin()) / tau * 1.4427 + 4 + 9) * U32
+    rq = (6 * reach + 8 + v / 256 + 32) * U32       # a sum by 256 threads and one exponential
+    low = lse.double().abs() < 1024
+    rq = rq + torch.where(low, 4 * U32 * (lse.double().abs() + moved.double().abs().amax(1) / tau) * 1.4427, 0.0)
+    g = tau * rg.double()[:, None]
+    tol = g * (q * (rq[:, None] + 4 * U32) + whole * (2 * rt + 4 * U32)) + want.abs() * u(dtype) * 1.01
+    close(grad, want, tol, "gradient from lse")
