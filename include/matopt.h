@@ -293,7 +293,8 @@ int32_t mo_expert_weight_grad(const void *dy, int64_t lddy, const void *x, int64
  * A row without entries, or whose entries are all -inf, has loss 0 and a zero grad.
  * Entries of one row that name the same id count one by one in the loss and add up in
  * the gradient.  grad is written whole, in the logits' dtype, rows ldg values apart;
- * it must not overlap the logits (MO_ERR_INVALID).  1 <= k <= 1024, temperature > 0, vocab <= 2^28.
+ * it must not overlap the logits (MO_ERR_INVALID).  1 <= k <= 1024, vocab <= 2^28, temperature
+ * finite and at least 2^-126.
  * lse is rounded to fp32 (an infinity where it lies beyond).  A common offset of a row's
  * logits, exact in their dtype, changes neither loss nor gradient.
  * mo_distill_backward takes the lse of mo_distill_forward; a row whose lse is 1024 or more

@@ -322,7 +322,7 @@ void k_distill(DistillArgs a) {
   };
   repack();
 
-  // sums: exp z; e_j; e_j (u_j - z_j)
+  // sums: exp z; e_j; tau e_j (u_j - z_j)
   float s3[3] = {0.f, 0.f, 0.f};
   if constexpr (HOLD) {
     s3[0] = ex(xr);
@@ -350,9 +350,9 @@ void k_distill(DistillArgs a) {
     if (id >= 0) {
       const float d = te.e[j] - tmax;
       e = fast_exp2(d * (LOG2E * inv_tau));
-      // 2^-11: up to 1024 terms of the largest size (a logit of the type's lowest value)
-      // stay finite; the power of two is exact
-      if (e != 0.f) s3[2] += e * ((d - (to_f32(row.p[id]) - xm)) * inv_tau * 0x1p-11f);
+      // tau e_j (u_j - z_j).  2^-12: up to 1024 terms of the largest size (logits of the
+      // type's lowest value and of its highest) stay finite; the power of two is exact
+      if (e != 0.f) s3[2] += e * (d * 0x1p-12f - (to_f32(row.p[id]) * 0x1p-12f - xm * 0x1p-12f));
     }
     s3[1] += e;
     te.e[j] = e;
@@ -363,7 +363,9 @@ void k_distill(DistillArgs a) {
   const float log_s = logf(s3[0]);
   if (tid == 0) {
     a.lse[r] = xm * inv_tau + log_s;
-    a.loss[r] = live ? a.tau * a.tau * (s3[2] / S * 0x1p11f + log_s - logf(S)) : 0.f;
+    // in an order in which nothing passes fp32's ends that does not in the end
+    const float t12 = s3[2] / S, first = a.tau < 1.f ? t12 * (a.tau * 0x1p12f) : t12 * 0x1p12f * a.tau;
+    a.loss[r] = live ? first + a.tau * (a.tau * (log_s - logf(S))) : 0.f;
   }
   if constexpr (MODE == D_BOTH) {
     repack();

@@ -19,8 +19,9 @@ int check_distill(const void* logits, int64_t ldx, const void* ids, int32_t id_b
   if (vocab < 1 || vocab > (int64_t(1) << 28)) return fail(MO_ERR_INVALID, "vocab must be in [1, 2^28]");
   if (k < 1 || k > DISTILL_MAX_K)
     return fail(MO_ERR_INVALID, "teacher entries per row must be in [1, " + std::to_string(DISTILL_MAX_K) + "]");
-  if (!std::isfinite(temperature) || temperature <= 0.f)
-    return fail(MO_ERR_INVALID, "temperature must be finite and > 0");
+  // below, 1 / temperature overflows
+  if (!std::isfinite(temperature) || temperature < 0x1p-126f)
+    return fail(MO_ERR_INVALID, "temperature must be finite and at least 2^-126");
   if (ldx < vocab) return fail(MO_ERR_INVALID, "logits: the row pitch must be >= vocab");
   if (n > 0 && (!logits || !ids || !teacher)) return fail(MO_ERR_INVALID, "logits, indices or teacher is NULL");
   return MO_OK;

@@ -140,3 +140,30 @@ def test_gradient_from_lse_with_an_offset(gpu, dtype, unit, offset, tau, v):
     g = tau * rg.double()[:, None]
     tol = g * (q * (rq[:, None] + 4 * U32) + whole * (2 * rt + 4 * U32)) + want.abs() * u(dtype) * 1.01
     close(grad, want, tol, "gradient from lse")
+
+
+@pytest.mark.parametrize("dtype,tau", [(BF16, 0.25), (F32, 0.5), (F32, 0.9), (F32, 1.0), (F32, 1e-25), (F32, 2.0 ** -126)])
+def test_losses_near_the_ends_of_their_type(gpu, dtype, tau):
+    """A teacher that asks for logits of the type's lowest value, where the loss is as large
+    as they are, times tau; and temperatures whose square is not a float."""
+    tau32 = float(torch.tensor(tau, dtype=F32))
+    x = torch.randn(3, 3000, generator=generator(gpu, 5), device=gpu).to(dtype)
+    if tau > 0.1:
+        x[:, 100:] = torch.finfo(dtype).min
+    idx = torch.arange(95, 104, device=gpu).expand(3, 9).contiguous()
+    t = torch.randn(3, 9, generator=generator(gpu, 6), device=gpu)
+    loss, _ = mo.distill_forward(x, idx, t, temperature=tau)
+    d = t.double() - t.double().amax(1, keepdim=True)
+    away = torch.gather(x, 1, idx).double() - x.double().amax(1, keepdim=True)
+    p = torch.softmax(d / tau32, 1)
+    log_q = torch.log_softmax(x.double() / tau32, 1)
+    assert bool(torch.isfinite(log_q).all())
+    log_p = torch.log_softmax(d / tau32, 1)
+    want = tau32 * tau32 * torch.where(p > 0, p * (log_p - torch.gather(log_q, 1, idx)), 0.0).sum(1)
+    assert bool((want > 0).all()) and float(want.max()) < torch.finfo(F32).max
+    # The sum's terms are off by the rounding of their weight (an exponent of d / tau, three
+    # roundings of its size), of the sums of 9, and ten more; a weight below fp32's smallest
+    # may be lost.
+    rt = torch.where(p > 1e-38, 3 * (d / tau32).abs() * 1.4427 * U32, 1.0)
+    size = (p * (d - away).abs() * (rt + (rt * p).sum(1, keepdim=True) + 32 * U32)).sum(1) * tau32
+    close(loss, want, size + tau32 * tau32 * 64 * U32 * 16, "loss")

@@ -201,3 +201,12 @@ def test_distill_refuses_a_gradient_over_the_logits():
             a = args(f, logits, ld, grad, ldg)
             if not torch.cuda.is_available():
                 assert call(f, *a) != INVALID, error()
+
+
+def test_distill_refuses_temperatures_without_a_reciprocal():
+    for tau in (2.0 ** -127, 2.0 ** -149):
+        refused(INVALID, "temperature", "mo_distill_forward", FAKE, 100, FAKE, 8, FAKE, 4, 100, 8, 0, tau, FAKE, FAKE, None)
+        refused(INVALID, "temperature", "mo_distill_backward", FAKE, 100, FAKE, FAKE, 8, FAKE, FAKE, 4, 100, 8, 0, tau,
+                FAKE << 8, 100, None)
+        refused(INVALID, "temperature", "mo_distill_forward_backward", FAKE, 100, FAKE, 8, FAKE, FAKE, 4, 100, 8, 0, tau,
+                FAKE, FAKE, FAKE << 8, 100, None)
