@@ -46,6 +46,7 @@ struct DistillArgs {
   float* lse;
   void* grad;           // n x V, pitch ldg
   int64_t ldg;
+  int64_t first_row;    // of this launch
 };
 
 __device__ inline float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -243,7 +244,7 @@ void k_distill(DistillArgs a) {
   const Teacher te(dyn, a.k);
   __shared__ __attribute__((aligned(16))) u32x4_t more[NL > 0 ? NL : 1][NL > 0 ? NT : 1];
   const uint32_t tid = threadIdx.x;
-  const int64_t r = blockIdx.x;
+  const int64_t r = a.first_row + blockIdx.x;
   const Row<T> row(static_cast<const T*>(a.x) + r * a.ldx, a.V);
   const float inv_tau = 1.f / a.tau;
   constexpr float NINF = -__builtin_inff();
@@ -453,7 +454,7 @@ __global__ __launch_bounds__(NT) void k_distill_backward(DistillArgs a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char dyn[];
   const Teacher te(dyn, a.k);
   const uint32_t tid = threadIdx.x;
-  const int64_t r = blockIdx.y;
+  const int64_t r = a.first_row + blockIdx.y;
   const Row<T> row(static_cast<const T*>(a.x) + r * a.ldx, a.V);
   const uint32_t from = blockIdx.x * (NT * NV), to = min(row.F, from + NT * NV);
   const bool last = blockIdx.x + 1 == gridDim.x;   // also holds the elements behind the pieces

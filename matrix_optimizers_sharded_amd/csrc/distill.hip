@@ -39,47 +39,41 @@ int check_grad(const void* logits, int64_t ldx, const void* grad, int64_t ldg, i
 template <typename T, int MODE>
 int run_rows(const DistillArgs& a, hipStream_t stream) {
   const int64_t pieces = a.V / RowVec<T>::N;
-  const dim3 grid(a.n);
-  return launch(PK_DISTILL, stream, [&] {
-#define MO_ROWS(NT, NR, NL) \
-  hipLaunchKernelGGL((k_distill<T, MODE, NT, NR, NL>), grid, dim3(NT), teacher_bytes(a.k), stream, a)
-    // A row over threads that hold 4 to 16 pieces each: many waves with few registers
-    // overlap their loads and exponentials best, idle pieces cost their share.  8192 rows of
-    // 32768 bf16 logits, loss and gradient: 215 us with 512 threads, 232 with 256, 263 with
-    // 1024; 6000 rows of 50257: 281 us with 13 pieces a thread, 298 with 16, 396 with 8 of
-    // 1024 threads.
-    if (pieces <= 64 * 4) MO_ROWS(64, 4, 0);
-    else if (pieces <= 128 * 8) MO_ROWS(128, 8, 0);
-    else if (pieces <= 256 * 8) MO_ROWS(256, 8, 0);
-    else if (pieces <= 512 * 6) MO_ROWS(512, 6, 0);
-    else if (pieces <= 512 * 8) MO_ROWS(512, 8, 0);
-    else if (pieces <= 512 * 13) MO_ROWS(512, 13, 0);
-    else if (pieces <= 512 * 16) MO_ROWS(512, 16, 0);
-    else if (pieces <= 512 * 32) MO_ROWS(512, 23, 9);
-    else MO_ROWS(512, 0, 0);
+#define MO_ROWS(NT, NR, NL)                                                                                     \
+  return launch_blocks(PK_DISTILL, stream, a.n, NT, [&](int64_t first, uint32_t count) {                         \
+    DistillArgs b = a;                                                                                          \
+    b.first_row = first;                                                                                        \
+    hipLaunchKernelGGL((k_distill<T, MODE, NT, NR, NL>), dim3(count), dim3(NT), teacher_bytes(a.k), stream, b); \
+  })
+  // A row over threads that hold 4 to 16 pieces each: many waves with few registers
+  // overlap their loads and exponentials best, idle pieces cost their share.  8192 rows of
+  // 32768 bf16 logits, loss and gradient: 215 us with 512 threads, 232 with 256, 263 with
+  // 1024; 6000 rows of 50257: 281 us with 13 pieces a thread, 298 with 16, 396 with 8 of
+  // 1024 threads.
+  if (pieces <= 64 * 4) MO_ROWS(64, 4, 0);
+  if (pieces <= 128 * 8) MO_ROWS(128, 8, 0);
+  if (pieces <= 256 * 8) MO_ROWS(256, 8, 0);
+  if (pieces <= 512 * 6) MO_ROWS(512, 6, 0);
+  if (pieces <= 512 * 8) MO_ROWS(512, 8, 0);
+  if (pieces <= 512 * 13) MO_ROWS(512, 13, 0);
+  if (pieces <= 512 * 16) MO_ROWS(512, 16, 0);
+  if (pieces <= 512 * 32) MO_ROWS(512, 23, 9);
+  MO_ROWS(512, 0, 0);
 #undef MO_ROWS
-  });
 }
 
 template <typename T>
 int run_backward(const DistillArgs& a, hipStream_t stream) {
   const int64_t per = 256 * 8;   // pieces a block
-  int64_t done = 0;   // rows of earlier launches (a grid holds 65535 of them)
-  while (done < a.n) {
+  const int64_t parts = cdiv(std::max<int64_t>(a.V / RowVec<T>::N, 1), per);
+  constexpr int64_t MOST = 65535;   // rows of a grid
+  for (int64_t first = 0; first < a.n; first += MOST) {
     DistillArgs b = a;
-    const int64_t rows = a.n - done < 65535 ? a.n - done : 65535;
-    b.x = static_cast<const T*>(a.x) + done * a.ldx;
-    b.ids = static_cast<const unsigned char*>(a.ids) + done * a.k * (a.ids64 ? 8 : 4);
-    b.t = a.t + done * a.k;
-    b.row_grad = a.row_grad + done;
-    b.lse_in = a.lse_in + done;
-    b.grad = static_cast<T*>(a.grad) + done * a.ldg;
-    b.n = rows;
+    b.first_row = first;
     MO_TRY(launch(PK_DISTILL, stream, [&] {
-      const int64_t parts = cdiv(std::max<int64_t>(a.V / RowVec<T>::N, 1), per);
-      hipLaunchKernelGGL((k_distill_backward<T, 256, 8>), dim3(parts, rows), dim3(256), teacher_bytes(a.k), stream, b);
+      hipLaunchKernelGGL((k_distill_backward<T, 256, 8>), dim3(parts, std::min(MOST, a.n - first)), dim3(256),
+                         teacher_bytes(a.k), stream, b);
     }));
-    done += rows;
   }
   return MO_OK;
 }
@@ -96,7 +90,7 @@ int32_t mo_distill_forward(const void* logits, int64_t ldx, const void* indices,
     if (n == 0) return MO_OK;
     if (!loss || !lse) return fail(MO_ERR_INVALID, "loss or lse is NULL");
     DistillArgs a = {logits, ldx, indices, teacher, vocab, n, static_cast<int>(k), index_bytes == 8, temperature,
-                     nullptr, nullptr, loss, lse, nullptr, 0};
+                     nullptr, nullptr, loss, lse, nullptr, 0, 0};
     if (dtype == MO_F32) return run_rows<float, D_FWD>(a, static_cast<hipStream_t>(stream));
     return run_rows<bf16_t, D_FWD>(a, static_cast<hipStream_t>(stream));
   });
@@ -113,7 +107,7 @@ int32_t mo_distill_backward(const void* logits, int64_t ldx, const float* lse, c
     if (!lse || !row_grad || !grad) return fail(MO_ERR_INVALID, "lse, row_grad or grad is NULL");
     MO_TRY(check_grad(logits, ldx, grad, ldg, n, vocab, dtype));
     DistillArgs a = {logits, ldx, indices, teacher, vocab, n, static_cast<int>(k), index_bytes == 8, temperature,
-                     row_grad, lse, nullptr, nullptr, grad, ldg};
+                     row_grad, lse, nullptr, nullptr, grad, ldg, 0};
     if (dtype == MO_F32) return run_backward<float>(a, static_cast<hipStream_t>(stream));
     return run_backward<bf16_t>(a, static_cast<hipStream_t>(stream));
   });
@@ -130,7 +124,7 @@ int32_t mo_distill_forward_backward(const void* logits, int64_t ldx, const void*
     if (!loss || !lse || !row_grad || !grad) return fail(MO_ERR_INVALID, "loss, lse, row_grad or grad is NULL");
     MO_TRY(check_grad(logits, ldx, grad, ldg, n, vocab, dtype));
     DistillArgs a = {logits, ldx, indices, teacher, vocab, n, static_cast<int>(k), index_bytes == 8, temperature,
-                     row_grad, nullptr, loss, lse, grad, ldg};
+                     row_grad, nullptr, loss, lse, grad, ldg, 0};
     if (dtype == MO_F32) return run_rows<float, D_BOTH>(a, static_cast<hipStream_t>(stream));
     return run_rows<bf16_t, D_BOTH>(a, static_cast<hipStream_t>(stream));
   });

@@ -51,6 +51,7 @@ struct XArgs {
   int32_t experts, k, m;
   int32_t vec_out;          // results can be stored 16 bytes at a time (aligned rows)
   int32_t slots;            // blocks that the device runs at a time
+  int64_t first_block;      // of this launch
 };
 
 // N 16-byte-per-lane loads straight into LDS (see load_lds16x4).
@@ -611,7 +612,7 @@ __device__ inline bool x_tile(const XArgs& a, unsigned char* smem, XTile& t, int
   if constexpr (KIND == X_DW) {
     const int ti = (a.m + TM - 1) / TM;
     const int64_t per = static_cast<int64_t>(ti) * ct, total = per * a.experts;
-    part = x_part<SPLITS>(blockIdx.x, total, a.slots);
+    part = x_part<SPLITS>(a.first_block + blockIdx.x, total, a.slots);
     if (part.item < 0) return false;
     t.e = static_cast<int>(part.item / per);
     int i, j;
@@ -627,7 +628,7 @@ __device__ inline bool x_tile(const XArgs& a, unsigned char* smem, XTile& t, int
     XSegs& s = *reinterpret_cast<XSegs*>(smem);
     x_segments<TM>(a, ct, s);
     const int S = a.experts + 2, total = s.begin[S];
-    part = x_part<SPLITS>(blockIdx.x, total, a.slots);
+    part = x_part<SPLITS>(a.first_block + blockIdx.x, total, a.slots);
     if (part.item < 0) return false;
     const int item = static_cast<int>(part.item);
     int lo = 0, hi = S - 1;   // the last segment that begins at or before the item

@@ -59,20 +59,21 @@ int launch_tile(int pk, XArgs a, hipStream_t stream) {
   const int64_t tiles = most_tiles<KIND, TM, TN>(a);
   if (tiles == 0) return MO_OK;
   const int64_t blocks = x_blocks(tiles, G::SPLITS, a.slots);
-  if (blocks > 0x7fffffffLL) return fail(MO_ERR_INVALID, "too many tiles for one launch");
-  return launch(pk, stream, [&] {
-    hipLaunchKernelGGL((k_expert<G, KIND>), dim3(static_cast<uint32_t>(blocks)), dim3(G::NT), 0, stream, a);
+  if (blocks > 0x7fffffffLL) return fail(MO_ERR_INVALID, "too many tiles");
+  return launch_blocks(pk, stream, blocks, G::NT, [&](int64_t first, uint32_t count) {
+    a.first_block = first;
+    hipLaunchKernelGGL((k_expert<G, KIND>), dim3(count), dim3(G::NT), 0, stream, a);
   });
 }
 
 template <typename T, int KIND, typename TO, int LOAD>
-int launch_split(int pk, const XArgs& a, hipStream_t stream) {
+int launch_split(int pk, XArgs a, hipStream_t stream) {
   typedef XSplit<T, KIND, TO, LOAD, 4> G;
   const int64_t tiles = most_tiles<KIND, G::TM, G::TN>(a);
-  if (tiles > 0x7fffffffLL) return fail(MO_ERR_INVALID, "too many tiles for one launch");
-  if (tiles == 0) return MO_OK;
-  return launch(pk, stream, [&] {
-    hipLaunchKernelGGL((k_expert_split<G, KIND>), dim3(static_cast<uint32_t>(tiles)), dim3(G::NT), 0, stream, a);
+  if (tiles > 0x7fffffffLL) return fail(MO_ERR_INVALID, "too many tiles");
+  return launch_blocks(pk, stream, tiles, G::NT, [&](int64_t first, uint32_t count) {
+    a.first_block = first;
+    hipLaunchKernelGGL((k_expert_split<G, KIND>), dim3(count), dim3(G::NT), 0, stream, a);
   });
 }
 

@@ -98,6 +98,19 @@ int launch(int pk, hipStream_t stream, F&& f) {
   return MO_OK;
 }
 
+// `blocks` blocks of `threads` threads as launches that the device can hold: a grid of 2^32
+// threads or more wraps, without an error.  f(first block, blocks of this launch).
+template <typename F>
+int launch_blocks(int pk, hipStream_t stream, int64_t blocks, int64_t threads, F&& f) {
+  const int64_t most = (int64_t(1) << 31) / threads;
+  for (int64_t first = 0; first < blocks; first += most) {
+    const int64_t count = blocks - first < most ? blocks - first : most;
+    const int rc = launch(pk, stream, [&] { f(first, static_cast<uint32_t>(count)); });
+    if (rc != MO_OK) return rc;
+  }
+  return MO_OK;
+}
+
 #define MO_TRY(x)            \
   do {                       \
     int rc_ = (x);           \

@@ -417,10 +417,10 @@ __device__ inline void zero_row(T* row, int width) {
 // table.  One wave per row.
 template <typename T, typename TO, bool WIDE>
 __global__ __launch_bounds__(256) void k_embed_lookup(const T* __restrict__ table, int64_t ldt, KeySource tokens,
-                                                      int64_t n, int dim, float scale,
+                                                      int64_t first_block, int64_t n, int dim, float scale,
                                                       TO* __restrict__ out) {
   const int lane = threadIdx.x & 63;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t i = (first_block + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (i >= n) return;
   const uint32_t tok = __builtin_amdgcn_readfirstlane(load_key(tokens, i));
   TO* o = out + i * dim;
@@ -476,14 +476,16 @@ struct EmbedGrad {
   int pitch;               // dim rounded up to a multiple of 8
   int32_t* tail_to;        // [chunk]: the last chunk of the token that crosses its end, -1: none
   int64_t run_blocks;
+  int64_t first_block;     // of this launch
 };
 
 template <typename T, typename TO, bool WIDE>
 __global__ __launch_bounds__(256) void k_embed_grad(EmbedGrad a) {
   const int lane = threadIdx.x & 63;
-  if (static_cast<int64_t>(blockIdx.x) >= a.run_blocks) {
+  const int64_t block = a.first_block + blockIdx.x;
+  if (block >= a.run_blocks) {
     // zeros for tokens without rows: the block's threads run along the table row
-    const int64_t v0 = (static_cast<int64_t>(blockIdx.x) - a.run_blocks) * EG_ZERO;
+    const int64_t v0 = (block - a.run_blocks) * EG_ZERO;
 #pragma unroll
     for (int r = 0; r < EG_ZERO; ++r) {
       const int64_t v = v0 + r;
@@ -493,7 +495,7 @@ __global__ __launch_bounds__(256) void k_embed_grad(EmbedGrad a) {
     }
     return;
   }
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t item = block * 4 + (threadIdx.x >> 6);
   const int64_t kept = a.offsets[a.tokens.num_keys];
   const int64_t chunk = item / a.parts, p0 = chunk * EG_ROWS;
   const bool tells = lane == 0 && item % a.parts == 0 && p0 < a.n;   // for its chunk, once

@@ -182,11 +182,13 @@ int check_embed(int64_t n, int64_t vocab, int64_t dim, int32_t dtype, int32_t ou
 
 template <typename T, typename TO>
 int run_embed_grad(const EmbedGrad& a, int64_t blocks, hipStream_t stream) {
-  MO_TRY(launch(PK_EGRAD, stream, [&] {
+  MO_TRY(launch_blocks(PK_EGRAD, stream, blocks, 256, [&](int64_t first, uint32_t count) {
+    EmbedGrad b = a;
+    b.first_block = first;
     if (a.dim >= ROW_W)
-      hipLaunchKernelGGL((k_embed_grad<T, TO, true>), dim3(blocks), dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((k_embed_grad<T, TO, true>), dim3(count), dim3(256), 0, stream, b);
     else
-      hipLaunchKernelGGL((k_embed_grad<T, TO, false>), dim3(blocks), dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((k_embed_grad<T, TO, false>), dim3(count), dim3(256), 0, stream, b);
   }));
   if (a.n <= EG_ROWS) return MO_OK;   // one chunk: nothing crosses
   return launch(PK_EGRAD, stream, [&] {
@@ -230,10 +232,10 @@ int32_t mo_embedding_lookup(const void* table, int64_t ldt, const void* tokens, 
     if (!table || !out) return fail(MO_ERR_INVALID, "table or out is NULL");
     const KeySource src = {tokens, token_bytes == 8, static_cast<uint32_t>(vocab)};
     hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
-    return launch(PK_LOOKUP, stream, [&] {
+    return launch_blocks(PK_LOOKUP, stream, cdiv(n, 4), 256, [&](int64_t first, uint32_t count) {
 #define MO_LOOKUP_W(T, TO, W)                                                                                   \
-  hipLaunchKernelGGL((k_embed_lookup<T, TO, W>), dim3(cdiv(n, 4)), dim3(256), 0, stream, static_cast<const T*>(table), \
-                     ldt, src, n, static_cast<int>(dim), scale, static_cast<TO*>(out))
+  hipLaunchKernelGGL((k_embed_lookup<T, TO, W>), dim3(count), dim3(256), 0, stream, static_cast<const T*>(table), ldt, \
+                     src, first, n, static_cast<int>(dim), scale, static_cast<TO*>(out))
 #define MO_LOOKUP(T, TO)                        \
   do {                                          \
     if (dim >= ROW_W) MO_LOOKUP_W(T, TO, true); \
@@ -287,7 +289,8 @@ int32_t mo_embedding_grad(const void* grad_out, int64_t ldg, const void* tokens,
     ZeroFill zero = {grad, 0};
     if (zeroed) zero.bytes = vocab * dim * static_cast<int64_t>(dtype_size(grad_dtype));
     const int64_t blocks = a.run_blocks + (zeroed ? 0 : cdiv(vocab, EG_ZERO));
-    if (blocks > 0x7fffffffLL || cdiv(zero.bytes, ZERO_BLOCK) > 0x7fffff00LL)
+    // a table of 2^39 bytes, and rows of 2^40 elements, are more than the device holds
+    if (cdiv(zero.bytes, ZERO_BLOCK) >= (1 << 21) || cdiv(p.chunks, EJ_CHUNKS) * cdiv(dim, EJ_COLS) >= (1 << 24))
       return fail(MO_ERR_INVALID, "too many blocks for one launch");
     MO_TRY(run_group(PK_EGRAD, a.tokens, n, p.group, const_cast<int32_t*>(a.order), const_cast<int32_t*>(a.offsets),
                      ws + p.off_group, zero, stream));
