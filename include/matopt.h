@@ -270,7 +270,9 @@ int32_t mo_embedding_grad(const void *grad_out, int64_t ldg, const void *tokens,
  *                                                 (experts x m x k)
  * Rows of no expert (before offsets[0], from offsets[experts] on) get zeros in y and
  * dx; an expert without rows gets a zero dw.  offsets: experts + 1 ascending int32, as
- * mo_group_rows gives them.  dtype: MO_F32 or MO_BF16, products summed in fp32;
+ * mo_group_rows gives them; others are clamped to [0, n], y and dx then take one that lies
+ * below an earlier one as equal to the largest before it, and dw[e] sums no row where
+ * offsets[e + 1] < offsets[e].  dtype: MO_F32 or MO_BF16, products summed in fp32;
  * out_dtype: MO_F32, or MO_BF16 with bf16 operands (one rounding).  1 <= experts <=
  * 1024, 1 <= k, m <= 2^20, 0 <= n <= 2^31 - 1024, results contiguous. */
 int32_t mo_expert_matmul(const void *x, int64_t ldx, const void *w, const int32_t *offsets, int32_t experts,

@@ -13,8 +13,9 @@
 // once, to the output type.
 //
 // Segments come from the device, so the tile list does too: every block sums the
-// segments' tiles in LDS and finds its own.  Offsets are clamped to [0, n], so that a
-// bad table can give wrong rows but no access out of range.  Rows that no segment
+// segments' tiles in LDS and finds its own.  Offsets are clamped to [0, n] and made
+// ascending, so that a bad table can give wrong rows but no access out of range and no row
+// that nobody or more than one writes.  Rows that no segment
 // holds (before o[0], from o[E] on) get zeros: they are tiles with an empty sum.  An
 // expert without rows gets a zero weight gradient the same way.
 //
@@ -104,20 +105,34 @@ __device__ inline int clamp_row(int v, int64_t n) {
 }
 
 // Items (tiles) of X_FWD and X_DX: every segment's row tiles times `ct` column tiles,
-// as a running sum.  One wave, 64 segments at a time.
+// as a running sum.  One wave, 64 segments at a time.  A bound below an earlier one is
+// raised to it, so segments share no row and cover [0, n) whatever the table holds: every
+// row is written once, and the grid's bound (row_tiles) and 32-bit sums hold.
 template <int TM>
 __device__ inline void x_segments(const XArgs& a, int ct, XSegs& s) {
   const int lane = threadIdx.x & 63;
   const int S = a.experts + 2;
   if (threadIdx.x < 64) {
-    int run = 0;
+    int run = 0, top = 0;   // top: the end of the segments so far
     for (int s0 = 0; s0 < S; s0 += 64) {
       const int i = s0 + lane;
       int lo = 0, hi = 0;
       if (i < S) {
         lo = i == 0 ? 0 : clamp_row(a.offsets[i - 1], a.n);
         hi = i == S - 1 ? static_cast<int>(a.n) : clamp_row(a.offsets[i], a.n);
-        if (hi < lo) hi = lo;
+      }
+      if (__ballot(i < S && (hi < lo || lo < top)) != 0) {   // not for an ascending table
+        hi = max(hi, top);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const int up = __shfl_up(hi, d);
+          if (lane >= d) hi = max(hi, up);
+        }
+        lo = __shfl_up(hi, 1);
+        if (lane == 0) lo = top;
+      }
+      top = __shfl(hi, 63);
+      if (i < S) {
         s.lo[i] = lo;
         s.hi[i] = hi;
       }
