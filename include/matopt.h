@@ -234,7 +234,8 @@ int32_t mo_plan_owners(const int64_t *rows, const int64_t *cols, int32_t count, 
  * device pointers, work enqueued on `stream`, no allocation, arguments checked on the
  * host before anything is launched.  What the host cannot see (keys, tokens, ids and
  * offsets) is bounds-checked in the kernels: a bad value gives a defined result, never
- * an access out of range.  Every result is deterministic.  n == 0 is valid. */
+ * an access out of range.  Every result is deterministic.  n == 0 is valid.  A result
+ * must not overlap an input (MO_ERR_INVALID). */
 
 /* Rows in the order of their key (stable): order[p] is the row at position p, and the
  * rows of key v are positions offsets[v] .. offsets[v+1]-1.  Rows whose key lies outside

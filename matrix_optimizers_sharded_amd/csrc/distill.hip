@@ -30,8 +30,7 @@ int check_distill(const void* logits, int64_t ldx, const void* ids, int32_t id_b
 int check_grad(const void* logits, int64_t ldx, const void* grad, int64_t ldg, int64_t n, int64_t vocab,
                int32_t dtype) {
   const int64_t es = static_cast<int64_t>(dtype_size(dtype));
-  const __int128 px = ldx, pg = ldg;
-  if (overlap({logits, n, vocab * es, px * es}, {grad, n, vocab * es, pg * es}))
+  if (overlap(byte_rows(logits, n, vocab, ldx, es), byte_rows(grad, n, vocab, ldg, es)))
     return fail(MO_ERR_INVALID, "grad must not be logits, nor overlap them");
   return MO_OK;
 }

@@ -36,6 +36,13 @@ inline int check_expert(const char* pa, const void* A, int64_t lda, int64_t wa, 
   return MO_OK;
 }
 
+// The result, `rows` x `width`, and the operands' rows.
+inline int check_result(const void* C, int64_t rows, int64_t width, int32_t out_dtype, const ByteRows& a,
+                        const ByteRows& b, const int32_t* offsets, int32_t experts) {
+  return check_apart("the result", byte_rows(C, rows, width, width, dtype_size(out_dtype)),
+                     {a, b, byte_rows(offsets, 1, experts + 1, experts + 1, 4)});
+}
+
 // An operand that can be loaded straight into LDS: rows of `width` elements, `pitch` apart.
 inline bool direct_rows(const void* p, int64_t pitch, int64_t width, int64_t es) {
   return aligned16(p) && pitch * es % 16 == 0 && width * es % 16 == 0;

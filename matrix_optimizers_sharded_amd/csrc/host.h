@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -38,13 +39,23 @@ struct ByteRows {
 };
 // Whether two of them share memory.  Columns of one buffer side by side do not.
 inline bool overlap(const ByteRows& a, const ByteRows& b) {
-  if (a.rows <= 0 || b.rows <= 0) return false;
+  if (a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
   auto first = [](const ByteRows& r) { return static_cast<__int128>(reinterpret_cast<uintptr_t>(r.p)); };
   auto end = [&](const ByteRows& r) { return first(r) + (r.rows - 1) * r.pitch + r.width; };
   if (end(a) <= first(b) || end(b) <= first(a)) return false;
   if (a.pitch != b.pitch) return true;
   const __int128 apart = ((first(b) - first(a)) % a.pitch + a.pitch) % a.pitch;
   return apart < a.width || apart + b.width > a.pitch;
+}
+
+// A call's result and its inputs: kernels read an input while other blocks store.
+inline int check_apart(const char* what, const ByteRows& out, std::initializer_list<ByteRows> inputs) {
+  for (const ByteRows& in : inputs)
+    if (overlap(out, in)) return fail(MO_ERR_INVALID, std::string(what) + " must not overlap an input");
+  return MO_OK;
+}
+inline ByteRows byte_rows(const void* p, int64_t rows, int64_t width, int64_t pitch, int64_t es) {
+  return {p, rows, width * es, static_cast<__int128>(pitch) * es};
 }
 
 // ---- optional per-kernel timing ------------------------------------------------

@@ -215,6 +215,9 @@ int32_t mo_group_rows(const void* keys, int32_t key_bytes, int64_t n, int64_t nu
     if (!offsets || (n > 0 && !order)) return fail(MO_ERR_INVALID, "order or offsets is NULL");
     const GroupPlan p = plan_group(n, num_keys);
     MO_TRY(check_workspace(workspace, workspace_bytes, p.bytes));
+    const ByteRows in = byte_rows(keys, 1, n, n, key_bytes);
+    MO_TRY(check_apart("order", byte_rows(order, 1, n, n, 4), {in}));
+    MO_TRY(check_apart("offsets", byte_rows(offsets, 1, num_keys + 1, num_keys + 1, 4), {in}));
     const KeySource src = {keys, key_bytes == 8, static_cast<uint32_t>(num_keys)};
     return run_group(PK_GROUP, src, n, p, order, offsets, static_cast<unsigned char*>(workspace),
                      ZeroFill{nullptr, 0}, static_cast<hipStream_t>(stream));
@@ -230,6 +233,8 @@ int32_t mo_embedding_lookup(const void* table, int64_t ldt, const void* tokens, 
     if (ldt < dim) return fail(MO_ERR_INVALID, "table: the row pitch must be >= dim");
     if (n == 0) return MO_OK;
     if (!table || !out) return fail(MO_ERR_INVALID, "table or out is NULL");
+    MO_TRY(check_apart("out", byte_rows(out, n, dim, dim, dtype_size(out_dtype)),
+                       {byte_rows(table, vocab, dim, ldt, dtype_size(dtype)), byte_rows(tokens, 1, n, n, token_bytes)}));
     const KeySource src = {tokens, token_bytes == 8, static_cast<uint32_t>(vocab)};
     hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
     return launch_blocks(PK_LOOKUP, stream, cdiv(n, 4), 256, [&](int64_t first, uint32_t count) {
@@ -268,6 +273,8 @@ int32_t mo_embedding_grad(const void* grad_out, int64_t ldg, const void* tokens,
     if (!grad || (n > 0 && !grad_out)) return fail(MO_ERR_INVALID, "grad_out or grad is NULL");
     const EmbedPlan p = plan_embed(n, vocab, dim);
     MO_TRY(check_workspace(workspace, workspace_bytes, p.bytes));
+    MO_TRY(check_apart("grad", byte_rows(grad, vocab, dim, dim, dtype_size(grad_dtype)),
+                       {byte_rows(grad_out, n, dim, ldg, dtype_size(dtype)), byte_rows(tokens, 1, n, n, token_bytes)}));
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
     EmbedGrad a = {};

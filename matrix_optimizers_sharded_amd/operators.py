@@ -7,8 +7,8 @@ out), raw pointers and torch's current stream.  The definitions are in
 include/matopt.h.  Every call only enqueues work, so it can be captured into a graph;
 there a call that takes a workspace has to be given one that has already served a call of the
 same sizes, and nothing else is needed.  Rows of two-dimensional inputs may be padded
-(any row pitch, unit column stride); results are contiguous.  No call differentiates
-itself: the gradients are calls of their own.
+(any row pitch, unit column stride); results are contiguous and overlap no input.  No call
+differentiates itself: the gradients are calls of their own.
 """
 
 import ctypes
@@ -288,7 +288,7 @@ def distill_forward(logits, indices, teacher, temperature=1.0):
 
 def distill_backward(logits, lse, indices, teacher, row_grad, temperature=1.0, out=None):
     """Gradient of the logits for the rows' weights row_grad, from distill_forward's lse.
-    Not in place: out must not overlap the logits."""
+    Not in place."""
     dev, ld, ib, n, v, k, code = _distill(logits, indices, teacher, temperature, lse, row_grad)
     out = _result(out, (n, v), logits.dtype, dev, "out")
     _run("mo_distill_backward", dev, logits.data_ptr(), ld, lse.data_ptr(), indices.data_ptr(), ib,
@@ -298,7 +298,7 @@ def distill_backward(logits, lse, indices, teacher, row_grad, temperature=1.0, o
 
 def distill_forward_backward(logits, indices, teacher, row_grad, temperature=1.0, out=None):
     """(loss, lse, gradient of the logits) in one pass, where the rows' weights are known.
-    Not in place: out must not overlap the logits."""
+    Not in place."""
     dev, ld, ib, n, v, k, code = _distill(logits, indices, teacher, temperature, None, row_grad)
     loss, lse = teacher.new_empty(n), teacher.new_empty(n)
     out = _result(out, (n, v), logits.dtype, dev, "out")

@@ -210,3 +210,28 @@ def test_distill_refuses_temperatures_without_a_reciprocal():
                 FAKE << 8, 100, None)
         refused(INVALID, "temperature", "mo_distill_forward_backward", FAKE, 100, FAKE, 8, FAKE, FAKE, 4, 100, 8, 0, tau,
                 FAKE, FAKE, FAKE << 8, 100, None)
+
+
+def test_results_over_inputs_are_refused():
+    """Other blocks still read what one block overwrites."""
+    at, text = 0x100000, "must not overlap an input"
+    for out in (at, at + 196, at - 36):                      # 50 int32 keys, 10 result words
+        refused(INVALID, text, "mo_group_rows", at, 4, 50, 9, FAKE, out, None, 0, None)
+    refused(INVALID, text, "mo_group_rows", at, 8, 50, 9, at + 392, FAKE, None, 0, None)
+    # a table of 9 rows of 16 bf16 values 20 apart (352 bytes), 5 tokens of 8 bytes
+    for out in (at, at + 350, at - 159):
+        refused(INVALID, text, "mo_embedding_lookup", at, 20, FAKE, 8, 5, 9, 16, 1, 1, 1.0, out, None)
+    refused(INVALID, text, "mo_embedding_lookup", FAKE, 20, at, 8, 5, 9, 16, 1, 1, 1.0, at + 36, None)
+    for out in (at, at + 190, at - 286):                     # 5 rows 20 apart (192 bytes), 288 bytes of result
+        refused(INVALID, text, "mo_embedding_grad", at, 20, FAKE, 8, 5, 9, 16, 1, 1, 1.0, out, FAKE, 1 << 30, None)
+    refused(INVALID, text, "mo_embedding_grad", FAKE, 20, at, 8, 5, 9, 16, 1, 1, 1.0, at + 36, FAKE, 1 << 30, None)
+    # 10 rows of 64 bf16 values, 3 experts of 64 x 64, offsets of 16 bytes
+    far, off = 0x900000, 0x800000
+    for name, w_rows in (("mo_expert_matmul", 192), ("mo_expert_input_grad", 192)):
+        for out in (at, at + 1278, at - 1278, far, far + 128 * w_rows - 2, off, off + 14):
+            refused(INVALID, text, name, at, 64, far, off, 3, 10, 64, 64, 1, 1, out, None)
+    for out in (at, at + 1278, at - 24574, far, off, off + 14):
+        refused(INVALID, text, "mo_expert_weight_grad", at, 64, far, 64, off, 3, 10, 64, 64, 1, 1, out, None)
+    if not torch.cuda.is_available():      # apart: past this check, and no further without a GPU
+        for out in (at + 1280, at - 1280, far - 1280, far + 24576, off + 16):
+            assert call("mo_expert_matmul", at, 64, far, off, 3, 10, 64, 64, 1, 1, out, None) != INVALID, error()
