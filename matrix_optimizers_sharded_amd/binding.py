@@ -161,18 +161,45 @@ def workspace_bytes(shapes, compute):
     return n
 
 
+def _capturing(device):
+    """Whether device's current stream is being captured into a graph."""
+    import torch
+    if not isinstance(device, torch.device):
+        device = torch.device(device)
+    if device.type != "cuda" or not torch.cuda.is_initialized():
+        return False
+    if device.index is None or device.index == torch._C._cuda_getDevice():
+        return torch._C._cuda_isCurrentStreamCapturing()
+    with _on(device):
+        return torch._C._cuda_isCurrentStreamCapturing()
+
+
 class Workspace:
-    """Device scratch for the batched calls, grown on demand (torch allocation)."""
+    """Device scratch for the batched calls, grown on demand (torch allocation).
+
+    Calls that share one must be ordered, on one stream or by events.  A buffer that a
+    captured call got stays allocated when a later call needs a larger one, since the graph
+    writes to it on every replay: a Workspace has to live as long as such graphs."""
 
     def __init__(self, device):
         self.device = device
         self.buf = None
+        self._captured = False   # self.buf was handed out under capture
+        self._kept = []
 
     def get(self, nbytes):
         import torch
+        capturing = _capturing(self.device)
         if self.buf is None or self.buf.numel() < nbytes:
+            if self._captured:
+                self._kept.append(self.buf)
+            elif self.buf is not None and self.buf.is_cuda:
+                # ordered after every earlier call, on whichever stream they ran
+                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
             self.buf = None
+            self._captured = False
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+        self._captured |= capturing
         return self.buf
 
 

@@ -5,8 +5,9 @@ and the distillation loss against a teacher's top logits with its gradient.
 Argument marshalling only, as in binding.py: checks, result tensors (unless given as
 out), raw pointers and torch's current stream.  The definitions are in
 include/matopt.h.  Every call only enqueues work, so it can be captured into a graph;
-there a call that takes a workspace has to be given one that has already served a call of the
-same sizes, and nothing else is needed.  Rows of two-dimensional inputs may be padded
+there a call that takes a workspace is given one that has already served a call of the same
+sizes and that lives as long as the graph, and calls that share a workspace, replays among
+them, are ordered on one stream.  Rows of two-dimensional inputs may be padded
 (any row pitch, unit column stride); results are contiguous and overlap no input.  No call
 differentiates itself: the gradients are calls of their own.
 """
