@@ -6,9 +6,9 @@
 import concurrent.futures
 import glob
 import os
-import shutil
 import subprocess
 import sys
+import tempfile
 import time
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,33 +32,31 @@ FLAGS = [
 
 
 def build(verbose=False, extra=()):
-    os.makedirs(os.path.dirname(LIB), exist_ok=True)
-    tmp = LIB + ".tmp"
+    where = os.path.dirname(LIB)
+    os.makedirs(where, exist_ok=True)
     t0 = time.time()
-    log = []
-    # a fixed place: the compiler's ids for the code objects come from the object's path,
-    # and the same sources have to give the same code
-    objdir = os.path.join(PKG, "lib", "obj")
-    os.makedirs(objdir, exist_ok=True)
-    try:
+    # a folder of its own, so that builds at once do not share files
+    with tempfile.TemporaryDirectory(prefix="build-", dir=where) as tmp:
         def compile_one(src):
-            obj = os.path.join(objdir, os.path.basename(src) + ".o")
-            cmd = [HIPCC, *FLAGS, *extra, "-c", "-o", obj, src]
+            name = os.path.splitext(os.path.basename(src))[0]
+            obj = os.path.join(tmp, name + ".o")
+            # the unit's id in the code, which the compiler would make from the paths: the
+            # same sources have to give the same code wherever they are
+            cmd = [HIPCC, *FLAGS, *extra, f"-cuid={name}", "-c", "-o", obj, src]
             return obj, subprocess.run(cmd, capture_output=True, text=True)
 
         with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
             done = list(pool.map(compile_one, SOURCES))
         results = [r for _, r in done]
+        lib = os.path.join(tmp, os.path.basename(LIB))
         if all(r.returncode == 0 for r in results):
-            link = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-o", tmp, *[o for o, _ in done]]
+            link = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-o", lib, *[o for o, _ in done]]
             results.append(subprocess.run(link, capture_output=True, text=True))
         log = [r.stdout + r.stderr for r in results]
         if any(r.returncode != 0 for r in results):
             sys.stderr.write("".join(log))
             raise RuntimeError("hipcc failed building libmatopt.so")
-    finally:
-        shutil.rmtree(objdir, ignore_errors=True)
-    os.replace(tmp, LIB)
+        os.replace(lib, LIB)
     if verbose:
         sys.stderr.write("".join(log))
         print(f"built {LIB} in {time.time() - t0:.1f}s")
