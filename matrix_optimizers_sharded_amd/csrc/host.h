@@ -109,6 +109,9 @@ int launch(int pk, hipStream_t stream, F&& f) {
   return MO_OK;
 }
 
+// Most blocks of 256 threads of one launch (see launch_blocks).
+constexpr int64_t MAX_BLOCKS_256 = (int64_t(1) << 24) - 1;
+
 // `blocks` blocks of `threads` threads as launches that the device can hold: a grid of 2^32
 // threads or more wraps, without an error.  f(first block, blocks of this launch).
 template <typename F>

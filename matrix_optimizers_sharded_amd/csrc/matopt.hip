@@ -622,7 +622,7 @@ int32_t sign_pack_batched(const void* u, int32_t dtype, int32_t M, int64_t numel
   // a block covers 4 waves x PACK_LOADS loads x 64 lanes x 16 bytes
   const int64_t per_block = 256 * PACK_LOADS * (16 / dtype_size(dtype));
   const int64_t blocks = (numel + per_block - 1) / per_block;
-  if (blocks > 0x7fffffffLL) return fail(MO_ERR_INVALID, "numel too large");
+  if (blocks > MAX_BLOCKS_256) return fail(MO_ERR_INVALID, "numel too large");
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   // 16-byte loads when every worker's values start 16-byte aligned
   const int64_t stride = M > 1 ? u_stride : 0;
@@ -656,7 +656,7 @@ int32_t sign_vote(const uint32_t* packed, int32_t M, int64_t numel, uint32_t* ou
   if (quad && nwords / 4 >= VOTE_PAIR_GROUPS) quad = 2;
   const int64_t per_block = quad == 2 ? 512 : 256;   // groups or words
   const int64_t blocks = ((quad ? nwords / 4 : nwords) + per_block - 1) / per_block;
-  if (blocks > 0x7fffffffLL) return fail(MO_ERR_INVALID, "numel too large");
+  if (blocks > MAX_BLOCKS_256) return fail(MO_ERR_INVALID, "numel too large");
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   // the counter needs 2^LV > M: 4 bit planes up to 15 workers, 8 up to 255, else 16
   return launch(PK_VOTE, stream, [&] {
@@ -683,7 +683,7 @@ int32_t sign_unpack(const uint32_t* packed, int64_t numel, int32_t dtype, void* 
   if (!packed || !out) return fail(MO_ERR_INVALID, "packed or out is NULL");
   const int64_t per_block = 256 * UNPACK_PIECES * (16 / dtype_size(dtype));
   const int64_t blocks = (numel + per_block - 1) / per_block;
-  if (blocks > 0x7fffffffLL) return fail(MO_ERR_INVALID, "numel too large");
+  if (blocks > MAX_BLOCKS_256) return fail(MO_ERR_INVALID, "numel too large");
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   const int vec = aligned16(out) ? 1 : 0;
   return launch(PK_UNPACK, stream, [&] {
@@ -705,7 +705,7 @@ int32_t sign_apply(const uint32_t* packed, int64_t numel, int32_t dtype, void* w
   if (!std::isfinite(lr)) return fail(MO_ERR_INVALID, "lr must be finite");
   const int64_t per_block = 256 * SAPPLY_PIECES * (16 / dtype_size(dtype));
   const int64_t blocks = (numel + per_block - 1) / per_block;
-  if (blocks > 0x7fffffffLL) return fail(MO_ERR_INVALID, "numel too large");
+  if (blocks > MAX_BLOCKS_256) return fail(MO_ERR_INVALID, "numel too large");
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   const int vec = aligned16(weight) ? 1 : 0;
   return launch(PK_SAPPLY, stream, [&] {

@@ -235,3 +235,13 @@ def test_results_over_inputs_are_refused():
     if not torch.cuda.is_available():      # apart: past this check, and no further without a GPU
         for out in (at + 1280, at - 1280, far - 1280, far + 24576, off + 16):
             assert call("mo_expert_matmul", at, 64, far, off, 3, 10, 64, 64, 1, 1, out, None) != INVALID, error()
+
+
+def test_sign_calls_refuse_more_than_a_launch_holds():
+    """2^24 blocks of 256 threads are 2^32 threads, of which only the remainder would run."""
+    lib = mo.load_library()
+    for numel in ((1 << 40) + 1, 1 << 41):
+        for rc in (lib.sign_pack(FAKE, 0, numel, FAKE, None), lib.sign_pack_batched(FAKE, 1, 2, numel, numel, FAKE, None),
+                   lib.sign_vote(FAKE, 3, numel, FAKE, None, None), lib.sign_unpack(FAKE, numel, 1, FAKE, None),
+                   lib.sign_apply(FAKE, numel, 1, FAKE, 0.5, None)):
+            assert rc == INVALID and "too large" in error(), (numel, rc, error())
