@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define MATOPT_VERSION 113
+#define MATOPT_VERSION 114
 
 /* element types */
 enum { MO_F32 = 0, MO_BF16 = 1 };

@@ -17,8 +17,10 @@
 // threads (up to 64 of each), or, up to 256 KiB, those and LDS; longer rows are read twice.
 // Bound by HBM: 4096 rows of 131072 bf16 logits, loss and gradient, 421 us, 5.1 TB/s, more
 // than a copy's 4.8 (a kernel that read every row twice: 1154 us).  The forward pass alone,
-// 8192 rows of 32768: 94 us, 5.7 TB/s.  2051 such rows, which are two rounds of blocks and
-// three rows, take 94 us for the two calls, 4.4 TB/s.
+// 8192 rows of 32768: 95 us, 5.7 TB/s.  2051 such rows, which are two rounds of blocks and
+// three rows, take 95 us for the two calls, 4.3 TB/s.  Beyond 256 KiB the loss alone is still
+// read once, 2048 rows of 151936 bf16 logits 106 us, 5.9 TB/s; with the gradient 352 us, 3.5
+// TB/s of what it cannot do without (1024 rows of 131072 fp32 logits: 293 us, 3.7 TB/s).
 #pragma once
 
 #include <type_traits>

@@ -48,7 +48,8 @@ int run_rows(const DistillArgs& a, hipStream_t stream) {
   // overlap their loads and exponentials best, idle pieces cost their share.  8192 rows of
   // 32768 bf16 logits, loss and gradient: 215 us with 512 threads, 232 with 256, 263 with
   // 1024; 6000 rows of 50257: 281 us with 13 pieces a thread, 298 with 16, 396 with 8 of
-  // 1024 threads.
+  // 1024 threads.  (With the difference from the maximum folded into one instruction; as it
+  // is taken now, the first is 220.)
   if (pieces <= 64 * 4) MO_ROWS(64, 4, 0);
   if (pieces <= 128 * 8) MO_ROWS(128, 8, 0);
   if (pieces <= 256 * 8) MO_ROWS(256, 8, 0);

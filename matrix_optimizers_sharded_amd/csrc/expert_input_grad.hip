@@ -10,8 +10,8 @@ extern "C" int32_t mo_expert_input_grad(const void* dy, int64_t lddy, const void
     MO_TRY(check_expert("dy", dy, lddy, m, "w", w, k, k, offsets, experts, n, k, m, dtype, out_dtype, dx));
     if (n == 0) return MO_OK;
     const int64_t es = static_cast<int64_t>(dtype_size(dtype)), eo = static_cast<int64_t>(dtype_size(out_dtype));
-    MO_TRY(check_result(dx, n, k, out_dtype, byte_rows(dy, n, m, lddy, es), byte_rows(w, experts * m, k, k, es), offsets,
-                        experts));
+    MO_TRY(check_result(dx, n, k, out_dtype, byte_rows(dy, n, m, lddy, es), byte_rows(w, experts * m, k, k, es),
+                        offsets, experts));
     XCall c;
     c.a = {dy, w, dx, offsets, lddy, k, k, n, experts, static_cast<int32_t>(k), static_cast<int32_t>(m),
            aligned16(dx) && k * eo % 16 == 0};

@@ -10,8 +10,8 @@ extern "C" int32_t mo_expert_matmul(const void* x, int64_t ldx, const void* w, c
     MO_TRY(check_expert("x", x, ldx, k, "w", w, k, k, offsets, experts, n, k, m, dtype, out_dtype, y));
     if (n == 0) return MO_OK;
     const int64_t es = static_cast<int64_t>(dtype_size(dtype)), eo = static_cast<int64_t>(dtype_size(out_dtype));
-    MO_TRY(check_result(y, n, m, out_dtype, byte_rows(x, n, k, ldx, es), byte_rows(w, experts * m, k, k, es), offsets,
-                        experts));
+    MO_TRY(check_result(y, n, m, out_dtype, byte_rows(x, n, k, ldx, es), byte_rows(w, experts * m, k, k, es),
+                        offsets, experts));
     XCall c;
     c.a = {x, w, y, offsets, ldx, k, m, n, experts, static_cast<int32_t>(k), static_cast<int32_t>(m),
            aligned16(y) && m * eo % 16 == 0};

@@ -10,8 +10,8 @@ extern "C" int32_t mo_expert_weight_grad(const void* dy, int64_t lddy, const voi
     MO_TRY(check_expert("dy", dy, lddy, m, "x", x, ldx, k, offsets, experts, n, k, m, dtype, out_dtype, dw));
     if (!dw) return fail(MO_ERR_INVALID, "the result is NULL");   // written whole, without rows too
     const int64_t es = static_cast<int64_t>(dtype_size(dtype)), eo = static_cast<int64_t>(dtype_size(out_dtype));
-    MO_TRY(check_result(dw, experts * m, k, out_dtype, byte_rows(dy, n, m, lddy, es), byte_rows(x, n, k, ldx, es), offsets,
-                        experts));
+    MO_TRY(check_result(dw, experts * m, k, out_dtype, byte_rows(dy, n, m, lddy, es), byte_rows(x, n, k, ldx, es),
+                        offsets, experts));
     XCall c;
     c.a = {dy, x, dw, offsets, lddy, ldx, k, n, experts, static_cast<int32_t>(k), static_cast<int32_t>(m),
            aligned16(dw) && k * eo % 16 == 0};

@@ -24,7 +24,8 @@
 // X_DX / X_DW, 1.14 PFLOP/s; one expert and whole rounds of tiles, 8192^3: 1.25-1.28.  The
 // rest goes to ragged ends, the last round of tiles and each tile's own start and end (a
 // compute unit holds one 256 x 256 tile, so its stores overlap no product).  Few rows: the
-// weights' way from HBM, 48 rows over 8 experts, 2048 x 5632: 35 us, 5.3 TB/s.  Short sums: the
+// weights' way from HBM, 48 rows over 8 experts, 2048 x 5632: 35 us, 5.3 TB/s (29 with weights
+// that the caches still hold in part).  Short sums: the
 // weight gradients' stores.  Between them, 128 rows an expert, 2048 x 1400: 3.7 TB/s
 // (X_FWD), 5.6 (X_DW).
 #pragma once

@@ -85,23 +85,35 @@ int launch_split(int pk, XArgs a, hipStream_t stream) {
 }
 
 // Which kernel and tile.  A large tile reads its operands fewer times, a small one keeps
-// more compute units busy.  Times in us for forward / input gradient / weight gradient,
-// the other choice in brackets.
+// more compute units busy.  The segments' sizes are on the device, so the choice sees the
+// mean rows of an expert, idle experts among them.  Times in us for forward / input
+// gradient, operands in the caches where they fit, the other choice in brackets.
 // 1. Few rows per expert, or few tiles, and a sum of four slabs or more: four waves split
-//    the sum.  48 rows over 8 experts, 2048 x 5632, bf16: 28 (30) / 30 (36); one row:
-//    7.7 (15) / 13 (35); 1001 rows over 6 experts, 768 x 1000, fp32: 26 (33) / 24 (29).
-//    Weight gradients: 16384 rows, 512 x 768, 2 experts: 35 (52).  Eight waves were
-//    faster only for a single expert's 128 x 128 gradient: 36 (41), and slower elsewhere.
+//    the sum (64 x 64 tiles in brackets).  One row: 7.7 (15) / 13 (35).  16 experts, 2048 x
+//    2816, bf16: 32 rows each 30 (31) / 33 (34), 33 rows 36 (31) / 36 (34); fp32, 1024 x 2048: 32
+//    rows 27 (44) / 27 (54), 33 rows 45 (43) / 43 (54).  Few tiles: 1001 rows over 6
+//    experts, 768 x 1000, fp32: 26 (33) / 24 (29); 1024 rows, one expert, 2048 x 2048, two
+//    tiles a compute unit, fp32: 78 (80) / 78 (81), but bf16 25 (21) / 23 (20).  A sum of four
+//    slabs, 128 rows, 16 experts, 256 x 2816: 6.8 (7.1).
+//    Weight gradients: 2 experts of 1024 rows, bf16: 768 x 640, 240 tiles, 7.3 (8.4); 768 x
+//    768, 288 tiles, split 9.3, 64 x 64 10.1.  16384 rows, 512 x 768, 2 experts: 35 (52).
+//    Eight waves were faster only for a single expert's 128 x 128 gradient: 36 (41).
 // 2. Weight gradients with sums of one or two slabs are all stores: one slab in LDS, so
 //    that four blocks share a compute unit.  300 rows over 128 experts, 1024 x 2048: 100
-//    (122, two slabs).
-// 3. bf16, segments of 160 rows or more: 256 x 256.  16384 rows, 8 experts, 4096 x 11008:
-//    1290 (128 x 128: 1640) / 1310 (1680) / 1300 (1710).  With odd widths, through
+//    (122, two slabs).  64 experts of 128 rows: 72 (92; 256 x 256: 77), of 129: 86 (256 x 256: 86).
+// 3. bf16, segments of 160 rows or more: 256 x 256 (128 x 128 in brackets).  16384 rows, 8
+//    experts, 4096 x 11008: 1290 (1640) / 1310 (1680), weight gradient 1300 (1710).  32
+//    experts, 2048 x 2816: 96 rows each 100 (102) / 71 (75), 159 rows 110 (121) / 92 (117), 160
+//    rows 110 (125) / 92 (120), 320 rows 181 (167) / 174 (175).  With odd widths, through
 //    registers, 8192 rows, 4 experts, 4095 x 5631: 450 / 500 / 505.
-//    4096 rows over 32 experts keep 128 x 128 with 128 rows each.
-// 4. 128 x 128, or 64 x 64 where there would be fewer tiles than compute units.  fp32
-//    products, which take 16 times as long, want two tiles for each: 2000 rows, 2
-//    experts, 512 x 2048 (272 tiles): 43 (69).
+// 4. 128 x 128, or 64 x 64 where there would be fewer tiles than compute units (in
+//    brackets).  64 experts, 2048 x 1408, bf16: 47 rows each 94 (82) / 75 (83), 48 rows the
+//    same, 96 rows 109 (104) / 82 (115), 128 rows 112 (115) / 86 (123).  fp32 products, which take
+//    16 times as long, want two tiles for each: 2000 rows, 2 experts, 512 x 2048 (272
+//    tiles): 43 (69).
+// What the mean costs where few experts hold all rows, 2048 x 1408, bf16: 4 of 64, 16384
+// rows, nothing; 4 of 128, 16384 rows, 112 (256 x 256: 102) / 119 (99); 4 of 128, 4096 rows, 63
+// (128 x 128: 37) / 71 (40); 1 of 64, 2048 rows, 33 (256 x 256: 23) / 34 (23).
 template <typename T, int KIND, typename TO, int LOAD>
 int launch_loaded(int pk, const XArgs& a, hipStream_t stream) {
   const int64_t cus = device_cus();

@@ -6,7 +6,9 @@
 // rows on).  A key outside [0, num_keys) counts as num_keys: its rows come last.
 // Counts and ranks are integers, so the result is exact and the same every time.
 // Bound by launches: 256 rows 7.6 us (a launch alone takes 3.6), 524288 rows with one
-// digit 13.8 us, of which the count takes 3 and the move 12.
+// digit 13.8 us, of which the count takes 3 and the move, on half of the compute units, 12.
+// 9000 and 100000 rows over 50000 keys, five launches: 28 and 31 us.  524289 rows with one
+// digit, three launches, 18.7 us; 2000000 rows 45 us, over 50000 keys 110 us.
 //
 // The embedding's two calls are bound by HBM: 65536 rows of a 131072 x 4096 bf16 table,
 // 136 us for the lookup (5.2 TB/s) and 370 us for the gradient: 35 us of grouping, 315 us

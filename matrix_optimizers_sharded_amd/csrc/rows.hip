@@ -234,7 +234,8 @@ int32_t mo_embedding_lookup(const void* table, int64_t ldt, const void* tokens, 
     if (n == 0) return MO_OK;
     if (!table || !out) return fail(MO_ERR_INVALID, "table or out is NULL");
     MO_TRY(check_apart("out", byte_rows(out, n, dim, dim, dtype_size(out_dtype)),
-                       {byte_rows(table, vocab, dim, ldt, dtype_size(dtype)), byte_rows(tokens, 1, n, n, token_bytes)}));
+                       {byte_rows(table, vocab, dim, ldt, dtype_size(dtype)),
+                        byte_rows(tokens, 1, n, n, token_bytes)}));
     const KeySource src = {tokens, token_bytes == 8, static_cast<uint32_t>(vocab)};
     hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
     return launch_blocks(PK_LOOKUP, stream, cdiv(n, 4), 256, [&](int64_t first, uint32_t count) {
